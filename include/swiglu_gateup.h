@@ -347,9 +347,9 @@ size_t swiglu_fc1_workspace_size(void);
  *   ends          [experts] int32 on the device, non-decreasing, in [0, rows].
  *                 The host does not read them, so a call may be captured into a
  *                 graph and replayed with other sizes. Values outside [0, rows]
- *                 are clamped and decreasing ones leave groups empty: no access
- *                 leaves the operands, and the results of the rows concerned are
- *                 unspecified.
+ *                 are clamped, and a group begins at the largest end before its
+ *                 own, so a decreasing end leaves its group empty: no access
+ *                 leaves the operands or the workspace, whatever the values.
  *   a, y, dy, da  token matrices with their row strides (elements).
  *   w, ldw, w_expert_stride
  *                 weights: row j of expert e starts at w + e * w_expert_stride

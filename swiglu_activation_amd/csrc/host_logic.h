@@ -140,6 +140,16 @@ inline Fc1Pool fc1_pool(uint32_t tiles, int64_t cus, int64_t threads, uint32_t p
     return {n_fixed, (uint32_t)grid};
 }
 
+// End of a group of token rows that begins at `before` (0 <= before <= rows) and
+// whose end is given as `end`, of any value: at least its beginning, at most `rows`.
+// A group begins where the last one ends, so the groups of any ends, also decreasing
+// or negative ones, share no row, and hold `rows` at most together. The
+// bounds of the launches and of the workspaces rest on that.
+constexpr int32_t group_end(int32_t before, int32_t end, int32_t rows) {
+    const int32_t v = end < rows ? end : rows;
+    return v > before ? v : before;
+}
+
 // Row tiles of `tile` rows that any split of `rows` rows over `experts` groups
 // and the spare rows after them can need: every group but the empty ones ends
 // on at most one partial tile, and a tile holds at least one row.

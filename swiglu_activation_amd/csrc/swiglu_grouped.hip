@@ -56,16 +56,47 @@ struct GroupedArgs {
     bool stream;             // and it is written past them
 };
 
-__device__ __forceinline__ int64_t clamp_end(int64_t v, int64_t rows) {
-    return v < 0 ? 0 : v > rows ? rows : v;
+__device__ __forceinline__ uint32_t lane_of(uint32_t v, int w) {
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, w);
 }
 
-// Row range of expert e. Ends outside [0, rows] are clamped, so that no value
-// of theirs leads outside the operands.
-__device__ __forceinline__ void expert_rows(const GroupedArgs& P, int64_t e, int64_t& lo, int64_t& hi) {
-    lo = e == 0 ? 0 : clamp_end(P.ends[e - 1], P.rows);
-    hi = e == P.experts ? P.rows : clamp_end(P.ends[e], P.rows);
-    hi = hi < lo ? lo : hi;
+// v from another lane of the wave, chosen by a DPP control; `none` where there is no
+// such lane or its row of 16 is not in ROWS.
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ uint32_t from_lane(uint32_t none, uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, CTRL, ROWS, 0xf, false);
+}
+// The largest v of this lane and those before it (all lanes of the wave take part).
+__device__ __forceinline__ uint32_t max_scan(uint32_t v) {
+    auto with = [&](uint32_t o) { v = o > v ? o : v; };
+    with(from_lane<0x111>(0, v));            // within rows of 16: 1, 2, 4 and 8 lanes before
+    with(from_lane<0x112>(0, v));
+    with(from_lane<0x114>(0, v));
+    with(from_lane<0x118>(0, v));
+    with(from_lane<0x142, 0xa>(0, v));       // a row's last lane to the next row (rows 1 and 3)
+    with(from_lane<0x143, 0xc>(0, v));       // lane 31 to rows 2 and 3
+    return v;
+}
+
+// Row range of expert e, or of the spare rows (e == P.experts). A group begins at
+// the largest end before it (swiglu_host::group_end): no ends, whatever their values
+// and order, lead outside the operands or make two groups share a row. The groups
+// before expert `from` are known to end at row `begin`. All lanes of the wave take part.
+__device__ __forceinline__ void expert_rows(const GroupedArgs& P, int64_t e, int64_t& lo, int64_t& hi,
+                                            int64_t from = 0, int32_t begin = 0) {
+    const int32_t rows = (int32_t)P.rows;
+    if (from < e) {
+        const int lane = threadIdx.x & 63;
+        uint32_t m = (uint32_t)begin;
+#pragma unroll 4
+        for (int64_t b = from; b < e; b += 64) {
+            const uint32_t v = b + lane < e ? (uint32_t)swiglu_host::group_end(0, P.ends[b + lane], rows) : 0;
+            m = v > m ? v : m;
+        }
+        begin = (int32_t)lane_of(max_scan(m), 63);
+    }
+    lo = begin;
+    hi = e == P.experts ? rows : swiglu_host::group_end(begin, P.ends[e], rows);
 }
 
 // The workgroup's place in the launch order of `total` tiles, or `total` if
@@ -99,16 +130,22 @@ template <int TILE, bool SPARE = true>
 struct RowTiles {
     uint32_t l, h, mine, sum;            // lane's expert: rows, tiles, inclusive sum
     uint32_t total;                      // row tiles in all
+    uint32_t top;                        // end of the last expert held in the lanes
     int64_t base;                        // first expert held in the lanes
 
     static __device__ __forceinline__ int64_t groups(const GroupedArgs& P) { return P.experts + SPARE; }
+    // Experts b on, after those that the lanes hold (or from the first).
     __device__ __forceinline__ void scan(const GroupedArgs& P, int64_t b) {
         const int lane = threadIdx.x & 63;
         base = b;
-        int64_t lo = 0, hi = 0;
-        if (b + lane < groups(P)) expert_rows(P, b + lane, lo, hi);
-        l = (uint32_t)lo;                                 // rows fit 31 bits
-        h = (uint32_t)hi;
+        const uint32_t begin = b == 0 ? 0 : top;
+        uint32_t v = 0;                                   // rows fit 31 bits
+        if (b + lane < P.experts) v = (uint32_t)swiglu_host::group_end(0, P.ends[b + lane], (int32_t)P.rows);
+        if (SPARE && b + lane == P.experts) v = (uint32_t)P.rows;
+        v = max_scan(v);
+        h = v > begin ? v : begin;
+        l = from_lane<0x138>(begin, h);                   // the lane before
+        top = lane_of(h, 63);
         mine = sum = (h - l + TILE - 1) / TILE;
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) {
@@ -116,14 +153,13 @@ struct RowTiles {
             if (lane >= d) sum += o;
         }
     }
-    static __device__ __forceinline__ uint32_t lane_of(uint32_t v, int w) {
-        return (uint32_t)__builtin_amdgcn_readlane((int)v, w);
-    }
     __device__ __forceinline__ void init(const GroupedArgs& P) {
-        total = 0;
-        for (int64_t b = (groups(P) - 1) / 64 * 64; b >= 0; b -= 64) {    // ends on the first 64
-            scan(P, b);
-            total += lane_of(sum, 63);
+        scan(P, 0);
+        total = lane_of(sum, 63);
+        RowTiles later = *this;                           // (the first 64 stay in the lanes)
+        for (int64_t b = 64; b < groups(P); b += 64) {
+            later.scan(P, b);
+            total += lane_of(later.sum, 63);
         }
     }
     // Tile `place` (below total * f_tiles) of the launch order.

@@ -204,15 +204,20 @@ struct Schedule {
     uint32_t f_tiles, per, j;              // feature tiles; workgroups per XCD; this one's place
     uint32_t full0, nf, half0, nh, keep;   // this XCD's tiles; keep: large ones not cut
     int64_t base;                          // first expert held in the lanes
+    uint32_t top;                          // end of the last one
     uint32_t l, h, full, half, sfull, shalf;   // lane's expert: rows, tiles, inclusive sums
 
+    // Experts b on, after those that the lanes hold (or from the first).
     __device__ __forceinline__ void scan(const GroupedArgs& P, int64_t b) {
         const int lane = threadIdx.x & 63;
         base = b;
-        int64_t lo = 0, hi = 0;
-        if (b + lane < P.experts) expert_rows(P, b + lane, lo, hi);
-        l = (uint32_t)lo;
-        h = (uint32_t)hi;
+        const uint32_t begin = b == 0 ? 0 : top;
+        uint32_t v = 0;
+        if (b + lane < P.experts) v = (uint32_t)swiglu_host::group_end(0, P.ends[b + lane], (int32_t)P.rows);
+        v = max_scan(v);
+        h = v > begin ? v : begin;
+        l = from_lane<0x138>(begin, h);                  // the lane before
+        top = lane_of(h, 63);
         const uint32_t rest = (h - l) % 256;
         half = rest > 0 && rest <= 128 ? 1 : 0;
         full = (h - l) / 256 + (rest > 128 ? 1 : 0);
@@ -227,9 +232,6 @@ struct Schedule {
             }
         }
     }
-    static __device__ __forceinline__ uint32_t lane_of(uint32_t v, int w) {
-        return (uint32_t)__builtin_amdgcn_readlane((int)v, w);
-    }
     static __device__ __forceinline__ void eighth(uint32_t total, uint32_t x, uint32_t& first,
                                                   uint32_t& n) {
         const uint32_t q = total / kXcds, r = total % kXcds;
@@ -240,11 +242,13 @@ struct Schedule {
         f_tiles = tiles;
         per = gridDim.x / kXcds;
         j = blockIdx.x / kXcds;
-        uint32_t fulls = 0, halves = 0;
-        for (int64_t b = (P.experts - 1) / 64 * 64; b >= 0; b -= 64) {    // ends on the first 64
-            scan(P, b);
-            fulls += lane_of(sfull, 63);
-            halves += lane_of(shalf, 63);
+        scan(P, 0);
+        uint32_t fulls = lane_of(sfull, 63), halves = lane_of(shalf, 63);
+        Schedule later = *this;                          // (the first 64 stay in the lanes)
+        for (int64_t b = 64; b < P.experts; b += 64) {
+            later.scan(P, b);
+            fulls += lane_of(later.sfull, 63);
+            halves += lane_of(later.shalf, 63);
         }
         eighth(fulls * f_tiles, blockIdx.x % kXcds, full0, nf);
         eighth(halves * f_tiles, blockIdx.x % kXcds, half0, nh);
@@ -639,7 +643,8 @@ struct Worker {
     uint32_t i;                                          // number of the next job
     int stored;                                          // rows of the tile before (0: none)
 
-    __device__ __forceinline__ Job next() {
+    // The next job after L (the first: one of no rows).
+    __device__ __forceinline__ Job next(const Job& L) {
         Job J{};
         if constexpr (OP == kWgrad) {
             const uint32_t per = sched.f_tiles * (uint32_t)((P.n_t + 255) / 256);
@@ -650,10 +655,14 @@ struct Worker {
                 uint32_t tt, ft;
                 J.expert = place / per;
                 tile_in_expert(place % per, per / sched.f_tiles, sched.f_tiles, tt, ft);
-                int64_t lo, hi;
-                expert_rows(P, J.expert, lo, hi);
-                J.lo = __builtin_amdgcn_readfirstlane((int32_t)lo);
-                J.len = __builtin_amdgcn_readfirstlane((int32_t)(hi - lo));
+                J.lo = L.lo;
+                J.len = L.len;
+                if (L.tt == 0 || J.expert != L.expert) { // (the order's experts do not decrease)
+                    int64_t lo, hi;
+                    expert_rows(P, J.expert, lo, hi, L.tt == 0 ? 0 : L.expert + 1, L.lo + L.len);
+                    J.lo = __builtin_amdgcn_readfirstlane((int32_t)lo);
+                    J.len = __builtin_amdgcn_readfirstlane((int32_t)(hi - lo));
+                }
                 J.t0 = (int32_t)tt * 256;
                 J.t1 = (int32_t)P.n_t;
                 J.f0 = (int32_t)ft;
@@ -683,7 +692,7 @@ struct Worker {
         Tile<OP, OutT, TT> M(src, wf, wt);
         if (J.len > 0) M.multiply(stored);
         M.pin();
-        const Job N = next();
+        const Job N = next(J);
         float s[kRows / 32];
         load_scales<OP>(P, J, wt, s);
         start(N);
@@ -705,7 +714,7 @@ __global__ __launch_bounds__(kThreads) void grouped_tile_kernel(GroupedArgs P, u
     } else {
         W.sched.init(P, f_tiles);
     }
-    Job J = W.next();
+    Job J = W.next(Job{});
     W.start(J);
     while (J.tt != 0) {
         if constexpr (OP == kWgrad) J = W.template make<256>(J);

@@ -1,0 +1,73 @@
+"""The grouped products at the borders of what they take (needs an MI355X): ends of any
+value and order, more experts than a wave has lanes. Bounds as in test_gpu_grouped.py."""
+
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import swiglu_activation_amd as sw
+from tests.test_gpu_grouped import OPS, _ends, _inputs, _run, _say, _verify
+
+pytestmark = pytest.mark.gpu
+
+
+def _given(ends):
+    return torch.tensor(ends, dtype=torch.int32, device="cuda")
+
+
+# direct, general, split (whole vectors and others), tiles; the last two with more than 64 experts
+ANY_ENDS = [(9, 3, 72, 200), (50, 3, 35, 77), (300, 3, 512, 4096), (300, 3, 511, 4095), (2000, 3, 512, 1024),
+            (200, 70, 72, 136), (9000, 100, 512, 768)]
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("shape", ANY_ENDS, ids=lambda c: "-".join(map(str, c)))
+def test_ends_of_any_value_and_order(op, shape):
+    """A group begins at the largest end before it. Ends that decrease, are negative or past
+    the rows give the bits of the ends in order that they amount to, within a workspace of
+    exactly the size asked for."""
+    rows, experts, n, k = shape
+    gen = torch.Generator().manual_seed(rows + n)
+    t, f, scale = _inputs(op, rows, experts, n, k, 0, gen)
+    rng = np.random.default_rng(rows)
+    top = 2 ** 31 - 1
+    turns = [rows if e % 2 == 0 else 0 for e in range(experts)]
+    cases = [turns, turns[::-1], sorted(rng.integers(0, rows + 1, experts).tolist(), reverse=True),
+             rng.integers(-rows, 2 * rows + 1, experts).tolist(), [top, -top - 1] * (experts // 2) + [5] * (experts % 2),
+             [-1] * experts]
+    need = sw.swiglu_grouped_workspace_size({"dgrad": "mm_dgrad", "wgrad": "mm_wgrad"}.get(op, op), rows, experts, n, k)
+    guard = 1 << 20
+    ws = torch.full((need + guard,), 0x5a, dtype=torch.uint8, device="cuda")
+    for i, ends in enumerate(cases):
+        _say(f"[grouped bounds] {op} {shape} ends {i}, workspace {need}")
+        fixed = np.maximum.accumulate(np.clip(np.array(ends, dtype=np.int64), 0, rows)).tolist()
+        sizes = np.diff([0] + fixed).tolist()
+        want = _run(op, t, f, _given(fixed), scale)
+        got = _run(op, t, f, _given(ends), scale, workspace=ws[:need] if need else None)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want), i
+        assert bool((ws[need:] == 0x5a).all()), i
+        if i in (0, 3):
+            _verify(op, got, t, f, sizes, scale, f"{op} ends {i}")
+        whole = _run(op, t, f, _given(ends), scale, workspace=False)
+        _verify(op, whole, t, f, sizes, scale, f"{op} ends {i} without workspace")
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("shape", [(6600, 66, 512, 768), (9000, 130, 768, 640)], ids=lambda c: "-".join(map(str, c)))
+def test_more_experts_than_lanes(op, shape):
+    """Groups of about 100 rows in tiles of 128 and 256, the experts around the 64th (and the 128th) empty."""
+    rows, experts, n, k = shape
+    _say(f"[grouped bounds] {op} {shape}")
+    gen = torch.Generator().manual_seed(experts)
+    rng = np.random.default_rng(experts)
+    p = rng.dirichlet(np.ones(experts) * 2)
+    for e in (62, 63, 64, 65, 127, 128):
+        if e < experts - 1:
+            p[e] = 0
+    sizes = rng.multinomial(rows, p / p.sum()).tolist()
+    t, f, scale = _inputs(op, rows, experts, n, k, 5, gen)
+    got = _run(op, t, f, _ends(sizes), scale)
+    _verify(op, got, t, f, sizes, scale, op)
