@@ -158,6 +158,12 @@ inline int64_t grouped_row_tiles(int64_t rows, int64_t experts, int64_t tile) {
     return groups + (rows - groups) / tile;
 }
 
+// The reduction index a step after r, or len where there is none. (r + step itself may
+// pass 31 bits: a group holds up to 2^31 - 1 rows.)
+constexpr int32_t next_step(int32_t r, int32_t len, int32_t step) {
+    return len - r > step ? r + step : len;
+}
+
 }  // namespace swiglu_host
 
 #endif  // SWIGLU_HOST_LOGIC_H

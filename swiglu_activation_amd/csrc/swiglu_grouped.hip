@@ -577,13 +577,14 @@ __global__ __launch_bounds__(kGenThreads, 3) void grouped_general_kernel(Grouped
         u32x4 vf[kGenChunks], vt[kGenChunks];
         sf.load(0, len, vf);
         st.load(0, len, vt);
-        for (int32_t r = 0; r < len; r += kGenK) {
+        for (int32_t r = 0; r < len;) {
             sf.store(lds_f, vf);
             st.store(lds_t, vt);
             __syncthreads();
-            if (r + kGenK < len) {
-                sf.load(r + kGenK, len, vf);
-                st.load(r + kGenK, len, vt);
+            r = swiglu_host::next_step(r, len, kGenK);
+            if (r < len) {
+                sf.load(r, len, vf);
+                st.load(r, len, vt);
             }
 #pragma unroll
             for (int s = 0; s < kGenK / 16; ++s) {
