@@ -50,13 +50,15 @@ __device__ __forceinline__ void make(const GroupedArgs& P, const uint16_t* w, co
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int i16 = lane % 16, g = lane / 16;
-    // offsets of this lane's loads at the reduction's start
-    const uint32_t of = i16 < feats ? (uint32_t)(i16 * (int32_t)P.ldf * 2 + g * 16) : kOutside;
+    // Offsets of this lane's loads at the reduction's start, kOutside for features and rows
+    // that do not exist. ANY, whose strides have no bound that 32 bits would fit, goes by
+    // pointers: its offsets are that mark or 0.
+    const uint32_t of = i16 >= feats ? kOutside : ANY ? 0 : (uint32_t)(i16 * (int32_t)P.ldf * 2 + g * 16);
     uint32_t ot[MT];
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
         const int r = 16 * j + i16;
-        ot[j] = r < rows ? (uint32_t)(r * (int32_t)P.ldt * 2 + g * 16) : kOutside;
+        ot[j] = r >= rows ? kOutside : ANY ? 0 : (uint32_t)(r * (int32_t)P.ldt * 2 + g * 16);
     }
     const __amdgpu_buffer_rsrc_t rt = buffer(t);
     __amdgpu_buffer_rsrc_t rf[H];

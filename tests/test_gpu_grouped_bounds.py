@@ -71,3 +71,25 @@ def test_more_experts_than_lanes(op, shape):
     t, f, scale = _inputs(op, rows, experts, n, k, 5, gen)
     got = _run(op, t, f, _ends(sizes), scale)
     _verify(op, got, t, f, sizes, scale, op)
+
+
+@pytest.mark.parametrize("op", ["mm", "fc1", "dgrad"])
+@pytest.mark.parametrize("n,k", [(24, 40), (19, 37)])
+def test_strides_past_31_bits(op, n, k):
+    """Few rows whose strides, and their weights', put a row a multiple of 2^31 or 2^32
+    bytes from the first: 2^30 elements between token rows, 2^27 between weight rows
+    (the 8th feature of a tile is 2^31 bytes from the first)."""
+    _say(f"[grouped bounds] {op} long strides, n {n} k {k}")
+    gen = torch.Generator().manual_seed(n)
+    sizes = [3]
+    t, f, scale = _inputs(op, 3, 1, n, k, 0, gen)
+    big = torch.zeros((2 << 30) + 64, dtype=torch.bfloat16, device="cuda")
+    tv = big.as_strided((3, t.shape[1]), (1 << 30, 1))
+    tv.copy_(t)
+    _verify(op, _run(op, tv, f, _ends(sizes), scale), t, f, sizes, scale, op + " token rows far apart")
+    del tv, big
+    rows = f.shape[1]
+    big = torch.zeros(((rows - 1) << 27) + 64, dtype=torch.bfloat16, device="cuda")
+    fv = big.as_strided((1, rows, f.shape[2]), (big.numel(), 1 << 27, 1))
+    fv.copy_(f)
+    _verify(op, _run(op, t, fv, _ends(sizes), scale), t, f, sizes, scale, op + " weight rows far apart")
