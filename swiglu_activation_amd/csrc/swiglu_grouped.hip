@@ -831,7 +831,9 @@ bool direct_fits(Op op, int64_t rows, int64_t experts, int64_t n_f) {
 
 Path path_of(Op op, bool whole, bool large, int64_t rows, int64_t experts, int64_t n_f, int64_t n_t,
              int64_t n_r) {
-    if (experts == 0) return kGeneralPath;
+    // No product: the general kernel stores zeros (the others' epilogues a row's scale times zero, NaN
+    // where that is not finite).
+    if (experts == 0 || (op != kWgrad && n_r == 0)) return kGeneralPath;
     if (op == kWgrad) {
         // Short groups: 754 rows, E = 6, 328 x 176 into fp32: 9 general, 13 in tiles; 348, E = 43,
         // 2032 x 128 into fp32: 12 and 20; 33, E = 2, 7248 x 3800: 24 and 33; but 1000, E = 8,

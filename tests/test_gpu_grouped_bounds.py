@@ -93,3 +93,16 @@ def test_strides_past_31_bits(op, n, k):
     fv = big.as_strided((1, rows, f.shape[2]), (big.numel(), 1 << 27, 1))
     fv.copy_(f)
     _verify(op, _run(op, t, fv, _ends(sizes), scale), t, f, sizes, scale, op + " weight rows far apart")
+
+
+@pytest.mark.parametrize("rows,experts,n", [(5, 2, 16), (3000, 4, 4096), (70000, 4, 1024)])
+def test_a_reduction_of_length_zero_gives_zeros(rows, experts, n):
+    """Whatever the rows' scales are."""
+    _say(f"[grouped bounds] fc1 of no columns, rows {rows} n {n}")
+    a = torch.empty(rows, 0, dtype=torch.bfloat16, device="cuda")
+    w = torch.empty(experts, 2 * n, 0, dtype=torch.bfloat16, device="cuda")
+    scale = torch.full((rows,), float("nan"), device="cuda")
+    scale[::2] = float("inf")
+    ends = _given([rows // experts * (e + 1) for e in range(experts)])
+    assert not bool(sw.swiglu_grouped_fc1(a, w, ends, scale).any())
+    assert not bool(sw.swiglu_grouped_mm(a, w, ends).any())
