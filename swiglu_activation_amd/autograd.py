@@ -48,6 +48,7 @@ it into autograd.
 from __future__ import annotations
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import (swiglu_ckpt8_bwd, swiglu_ckpt8_fwd, swiglu_fc1_fwd, swiglu_gateup_bias_scale_bwd,
@@ -394,7 +395,10 @@ class GroupedSwiGLUMLP(torch.nn.Module):
         if a.dim() != 2:
             raise ValueError(f"GroupedSwiGLUMLP: expected [tokens, hidden], got {a.dim()}D")
         needs = [a, self.w1, self.w2] + ([weights] if weights is not None else [])
-        if torch.is_grad_enabled() and any(t.requires_grad for t in needs):
+        # (a forward-mode tangent too has to meet the Function: it refuses it)
+        if (torch.is_grad_enabled() and any(t.requires_grad for t in needs)) or \
+                (forward_ad._current_level >= 0 and
+                 any(forward_ad.unpack_dual(t).tangent is not None for t in needs)):
             return GroupedSwiGLUExperts.apply(a, self.w1, self.w2, ends, weights)
         y = swiglu_grouped_fc1(_as_row_view(a), self.w1, ends, _fp32_scale(weights))
         return swiglu_grouped_mm(y, self.w2, ends)
