@@ -1,5 +1,7 @@
-"""Compile the HIP library in-tree: csrc/*.hip -> libswiglu_gateup.so, and the module
-that calls it from torch tensors: csrc/torch_calls.cpp -> _torch_calls.so.
+"""Compile the HIP library in-tree: csrc/*.hip -> libswiglu_gateup.so, the C client, and
+the module that calls the library from torch tensors: csrc/torch_calls.cpp -> _torch_calls.so
+(where torch, its headers and a C++ compiler are at hand; the library and the client need none
+of them).
 
 gfx950 only. Packed-fp32 instruction selection is switched off for the device
 code (``-packed-fp32-ops``); the host pass prints a harmless warning about the
@@ -59,21 +61,35 @@ def build(verbose: bool = False) -> str:
     if verbose and err.strip():
         print(err, file=sys.stderr)
     os.replace(tmp, LIB)
-    build_calls(verbose)
     build_client(verbose)
+    build_calls(verbose)
     return LIB
 
 
-def build_calls(verbose: bool = False) -> str:
-    """Compile the CPython module (C++17, host compiler) against the library and torch."""
+def build_calls(verbose: bool = False):
+    """Compile the CPython module (C++17, host compiler) against the library and torch.
+    Returns its path, or None, with a note on stderr, where what it needs is missing: the
+    binding then makes those calls through ctypes."""
     import sysconfig
 
-    import torch
+    def without(what):
+        if os.path.exists(CALLS):
+            os.remove(CALLS)             # of an earlier build, perhaps of another library
+        print(f"_torch_calls.so is not built: {what}", file=sys.stderr)
+
+    try:
+        import torch
+    except ImportError:
+        return without("torch is not importable")
     cxx = shutil.which("g++") or shutil.which("c++")
     if cxx is None:
-        raise RuntimeError("no C++ compiler for the torch calls")
+        return without("no C++ compiler")
     rocm = os.path.dirname(os.path.dirname(os.path.realpath(hipcc())))
     tdir = os.path.dirname(os.path.abspath(torch.__file__))
+    for header in (os.path.join(tdir, "include", "ATen", "hip", "EmptyTensor.h"),
+                   os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        if not os.path.exists(header):
+            return without(f"no {header}")
     tlib = os.path.join(tdir, "lib")
     tmp = CALLS + ".tmp"
     cmd = [cxx, "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-Wall",
