@@ -747,6 +747,15 @@ def _scratch(need, like, stream):
         return torch.empty(need, dtype=torch.uint8, device=like.device)
 
 
+def _span_of_workspace(workspace, like):
+    """(pointer, bytes) of a caller's workspace: its elements have to be its memory (an
+    expanded view has more of them than bytes behind its pointer)."""
+    _require_device(workspace, like)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def _grouped_workspace(op, rows, e, n, k, workspace, like, stream):
     """(tensor kept alive for the call, pointer, bytes). workspace None: taken
     from torch's allocator, on the stream the kernels run on."""
@@ -757,8 +766,7 @@ def _grouped_workspace(op, rows, e, n, k, workspace, like, stream):
         workspace = _scratch(need, like, stream)
     elif workspace is False:
         return None, None, 0
-    _require_device(workspace, like)
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return (workspace, *_span_of_workspace(workspace, like))
 
 
 def swiglu_grouped_mm(a, w, ends, y=None, *, workspace=None, stream=None):
@@ -985,8 +993,7 @@ def swiglu_ckpt8_bwd(dy, q, qs, scale=None, dx=None, *, want_y: bool = False, wa
     need = lib.swiglu_ckpt8_workspace_size(rows, n, _dtype_code(dy)) if want_dscale else 0
     if workspace is None and need:
         workspace = _scratch(need, dy, stream)
-    wp, wb = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) \
-        if workspace is not None else (None, 0)
+    wp, wb = _span_of_workspace(workspace, dy) if workspace is not None else (None, 0)
     with _on_device(dy.device):
         st = lib.swiglu_ckpt8_bwd(dy.data_ptr(), dys, q.data_ptr(), qst, qs.data_ptr(), qss, sp, ss,
                                   dx.data_ptr(), dxs, yp, ys, dsp, dss, wp, wb, rows, n,
