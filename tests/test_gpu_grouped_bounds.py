@@ -1,5 +1,6 @@
 """The grouped products at the borders of what they take (needs an MI355X): ends of any
-value and order, more experts than a wave has lanes. Bounds as in test_gpu_grouped.py."""
+value and order, more experts than a wave has lanes, strides past 31 bits, reductions of
+length zero, gradients larger than the caches. Bounds as in test_gpu_grouped.py."""
 
 from __future__ import annotations
 
@@ -106,3 +107,19 @@ def test_a_reduction_of_length_zero_gives_zeros(rows, experts, n):
     ends = _given([rows // experts * (e + 1) for e in range(experts)])
     assert not bool(sw.swiglu_grouped_fc1(a, w, ends, scale).any())
     assert not bool(sw.swiglu_grouped_mm(a, w, ends).any())
+
+
+@pytest.mark.parametrize("dtype,k", [(torch.bfloat16, 4096), (torch.float32, 2048), (torch.float32, 4104),
+                                     (torch.bfloat16, 4104)])
+def test_weight_gradients_larger_than_the_caches(dtype, k):
+    """Short groups and more than 256 MiB of gradients: rows of whole 128-byte lines are
+    stored past the caches, others through them. Some experts have no rows."""
+    experts, n = 44, 1000
+    _say(f"[grouped bounds] wgrad {dtype} {experts} x {n} x {k}")
+    gen = torch.Generator().manual_seed(k)
+    sizes = np.random.default_rng(k).multinomial(1900, np.arange(experts) % 5 / (np.arange(experts) % 5).sum()).tolist()
+    assert experts * n * k * dtype.itemsize > 256 << 20 and 0 in sizes
+    t, f, _ = _inputs("wgrad", 1900, experts, n, k, 7, gen)
+    got = _run("wgrad", t, f, _ends(sizes), None, dtype)
+    _verify("wgrad", got, t, f, sizes, None, f"wgrad {dtype}")
+    assert torch.equal(got, _run("wgrad", t, f, _ends(sizes), None, dtype)), "two calls differ"
