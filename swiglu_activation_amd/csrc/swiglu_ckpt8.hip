@@ -6,9 +6,10 @@
 // of one half of a row becomes 32 e4m3 values q and one scale byte b with
 // x ~ q 2^(b - 127). b is the smallest value >= 1 whose scale brings the
 // block's largest finite magnitude to 448 (the largest e4m3 value) or below,
-// so no value saturates and, but for e4m3's own subnormal range, each is kept
-// to 4 significant bits. The backward reads q and b in x's place: per column
-// 2 + 2/32 bytes instead of 4 (bf16) or 8 (fp32).
+// so no value saturates and each within 2^-13 of the block's largest is kept to 4
+// significant bits (smaller ones may fall in e4m3's subnormal range: steps of 2^-9
+// scales). The backward reads q and b in x's place: per column 2 + 2/32 bytes instead
+// of 4 (bf16) or 8 (fp32).
 //
 // Design. As in the plain SwiGLU kernels the op is a stream: every lane owns
 // one 16-byte vector of x's gate half and the one of its up half. A block of 32

@@ -1,7 +1,7 @@
 // Device-side building blocks shared by the SwiGLU kernels (gfx950): vector
 // access of bf16 / fp32 rows, the sigmoid and silu' arithmetic, the launch
 // geometry, and the host-side argument checks common to every entry point.
-// Included by swiglu_gateup.hip and swiglu_bias_scale.hip.
+// Included by every .hip source here.
 #ifndef SWIGLU_DEVICE_H
 #define SWIGLU_DEVICE_H
 

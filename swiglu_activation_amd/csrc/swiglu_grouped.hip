@@ -777,7 +777,9 @@ int64_t split_len(Op op, int64_t rows, int64_t experts, int64_t n_r) {
 enum Path { kDirectPath, kSplitPath, kTilePath, kGeneralPath };
 
 // Estimates in us, of which the smallest is taken. They were fitted to (and the
-// comments give) the times of kernels that follow one another: direct, general, tiles.
+// comments give) the times of kernels that follow one another: direct, general, tiles. They
+// are to rank the kernels, and are off by up to 1.6 times in places (fc1, 1014 rows, E = 24, n = 176,
+// k = 2056: 23.5 for the direct kernel's 15; dgrad, 64 rows, E = 64, n = 1792, k = 4096: 291 for 188).
 struct Estimate {
     double direct, general, tiles, split;
 };
