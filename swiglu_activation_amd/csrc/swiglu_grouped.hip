@@ -88,9 +88,9 @@ __device__ __forceinline__ void expert_rows(const GroupedArgs& P, int64_t e, int
     if (from < e) {
         const int lane = threadIdx.x & 63;
         uint32_t m = (uint32_t)begin;
-#pragma unroll 4
         for (int64_t b = from; b < e; b += 64) {
-            const uint32_t v = b + lane < e ? (uint32_t)swiglu_host::group_end(0, P.ends[b + lane], rows) : 0;
+            const int64_t i = b + lane < e ? b + lane : e - 1;   // (the last one again)
+            const uint32_t v = (uint32_t)swiglu_host::group_end(0, P.ends[i], rows);
             m = v > m ? v : m;
         }
         begin = (int32_t)lane_of(max_scan(m), 63);

@@ -642,9 +642,9 @@ struct Worker {
     Operands<OP> src;
     uint32_t i;                                          // number of the next job
     int stored;                                          // rows of the tile before (0: none)
+    int32_t last, begin;                                 // wgrad: the last job's expert and its first row
 
-    // The next job after L (the first: one of no rows).
-    __device__ __forceinline__ Job next(const Job& L) {
+    __device__ __forceinline__ Job next() {
         Job J{};
         if constexpr (OP == kWgrad) {
             const uint32_t per = sched.f_tiles * (uint32_t)((P.n_t + 255) / 256);
@@ -655,14 +655,13 @@ struct Worker {
                 uint32_t tt, ft;
                 J.expert = place / per;
                 tile_in_expert(place % per, per / sched.f_tiles, sched.f_tiles, tt, ft);
-                J.lo = L.lo;
-                J.len = L.len;
-                if (L.tt == 0 || J.expert != L.expert) { // (the order's experts do not decrease)
-                    int64_t lo, hi;
-                    expert_rows(P, J.expert, lo, hi, L.tt == 0 ? 0 : L.expert + 1, L.lo + L.len);
-                    J.lo = __builtin_amdgcn_readfirstlane((int32_t)lo);
-                    J.len = __builtin_amdgcn_readfirstlane((int32_t)(hi - lo));
-                }
+                int64_t lo, hi;
+                // (the order's experts do not decrease)
+                expert_rows(P, J.expert, lo, hi, last, begin);
+                J.lo = __builtin_amdgcn_readfirstlane((int32_t)lo);
+                J.len = __builtin_amdgcn_readfirstlane((int32_t)(hi - lo));
+                last = J.expert;
+                begin = J.lo;
                 J.t0 = (int32_t)tt * 256;
                 J.t1 = (int32_t)P.n_t;
                 J.f0 = (int32_t)ft;
@@ -692,7 +691,7 @@ struct Worker {
         Tile<OP, OutT, TT> M(src, wf, wt);
         if (J.len > 0) M.multiply(stored);
         M.pin();
-        const Job N = next(J);
+        const Job N = next();
         float s[kRows / 32];
         load_scales<OP>(P, J, wt, s);
         start(N);
@@ -706,7 +705,7 @@ struct Worker {
 // The grid is a multiple of kXcds workgroups, at most one per CU.
 template <Op OP, typename OutT>
 __global__ __launch_bounds__(kThreads) void grouped_tile_kernel(GroupedArgs P, uint32_t f_tiles) {
-    Worker<OP, OutT> W{P, {}, {}, 0, 0};
+    Worker<OP, OutT> W{P, {}, {}, 0, 0, 0, 0};
     if constexpr (OP == kWgrad) {
         W.sched.f_tiles = f_tiles;
         W.sched.per = gridDim.x / kXcds;
@@ -714,7 +713,7 @@ __global__ __launch_bounds__(kThreads) void grouped_tile_kernel(GroupedArgs P, u
     } else {
         W.sched.init(P, f_tiles);
     }
-    Job J = W.next(Job{});
+    Job J = W.next();
     W.start(J);
     while (J.tt != 0) {
         if constexpr (OP == kWgrad) J = W.template make<256>(J);
