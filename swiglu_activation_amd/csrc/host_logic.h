@@ -158,11 +158,9 @@ inline int64_t grouped_row_tiles(int64_t rows, int64_t experts, int64_t tile) {
     return groups + (rows - groups) / tile;
 }
 
-// The reduction index a step after r, or len where there is none. (r + step itself may
-// pass 31 bits: a group holds up to 2^31 - 1 rows.)
-constexpr int32_t next_step(int32_t r, int32_t len, int32_t step) {
-    return len - r > step ? r + step : len;
-}
+// Whether a step of the reduction follows the one at index r. (r + step itself may pass 31
+// bits where none does: a group holds up to 2^31 - 1 rows.)
+constexpr bool more_steps(int32_t r, int32_t len, int32_t step) { return len - r > step; }
 
 }  // namespace swiglu_host
 

@@ -577,14 +577,14 @@ __global__ __launch_bounds__(kGenThreads, 3) void grouped_general_kernel(Grouped
         u32x4 vf[kGenChunks], vt[kGenChunks];
         sf.load(0, len, vf);
         st.load(0, len, vt);
-        for (int32_t r = 0; r < len;) {
+        for (int32_t r = 0;; r += kGenK) {
             sf.store(lds_f, vf);
             st.store(lds_t, vt);
             __syncthreads();
-            r = swiglu_host::next_step(r, len, kGenK);
-            if (r < len) {
-                sf.load(r, len, vf);
-                st.load(r, len, vt);
+            const bool more = swiglu_host::more_steps(r, len, kGenK);
+            if (more) {
+                sf.load(r + kGenK, len, vf);
+                st.load(r + kGenK, len, vt);
             }
 #pragma unroll
             for (int s = 0; s < kGenK / 16; ++s) {
@@ -601,6 +601,7 @@ __global__ __launch_bounds__(kGenThreads, 3) void grouped_general_kernel(Grouped
                         acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ff[i], ft[j], acc[i][j], 0, 0, 0);
             }
             __syncthreads();
+            if (!more) break;
         }
     }
 
